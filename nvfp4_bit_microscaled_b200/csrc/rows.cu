@@ -380,6 +380,7 @@ __device__ void quantize_rows_cluster(const uint16_t* __restrict__ x, int T, int
   __shared__ float r_tbl[kRTableSize];
   const int S = C / 16, blocks = T * S, stride = CTAS * kQuantThreads;
   const int first = static_cast<int>(rank) * kQuantThreads + threadIdx.x;
+  if (CTAS > 1) cluster_arrive();   // this CTA runs; its peers wait for that before they store into it
   uint4 keep[kQuantKeep][2];
   uint32_t m = 0;
 #pragma unroll
@@ -403,6 +404,7 @@ __device__ void quantize_rows_cluster(const uint16_t* __restrict__ x, int T, int
   m = __reduce_max_sync(0xFFFFFFFFu, m);
   if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = m;
   __syncthreads();
+  if (CTAS > 1) cluster_wait();   // every peer's shared memory exists
   if (threadIdx.x < 32) {
     m = threadIdx.x < kQuantThreads / 32 ? warp_max[threadIdx.x] : 0u;
     m = __reduce_max_sync(0xFFFFFFFFu, m);

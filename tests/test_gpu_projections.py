@@ -1,0 +1,55 @@
+"""The gated projection and the adapters where their kernels meet: clusters, overlapping launches, the side stream, many
+tiles for each CTA, and the ends of the value range."""
+import numpy as np
+import pytest
+import torch
+
+from nvfp4_bit_microscaled_b200 import api, synth
+from tests import _nvfp4_ref as R
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from nvfp4_bit_microscaled_b200 import build
+    build.build()
+    api.read_device_error(clear=True)
+    yield
+    torch.cuda.synchronize()
+    assert api.read_device_error(clear=True) == 0
+
+
+def _i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def _copies(w):
+    return api.quantize(w, api.TWO_D, api.amax(w))
+
+
+@pytest.mark.parametrize("T,C", [(2, 256), (40, 512), (100, 1088)])
+def test_few_rows_quantizer_clusters_under_load(T, C):
+    # clusters of 1, 8 and 16 CTAs take X's amax together; beside them other streams keep the SMs busy, so that the
+    # CTAs of a cluster begin apart: the same bytes every time
+    w = synth.weights(512, C, 1).cuda()
+    row, _ = _copies(w)
+    ad = api.LoraAdapters((torch.randn(2, 16, C) / 16).bfloat16().cuda(), torch.randn(2, 512, 16).bfloat16().cuda(),
+                          torch.ones(2, device="cuda"))
+    seg = _i32([0, T // 2, T]), _i32([1, 0])
+    xs = [synth.activations(T, C, 10 + i, outlier_scale=20.0 * (i + 1)).cuda() for i in range(3)]
+    want = [(api.gated_apply(x, row), api.lora_fwd(x, row, ad, *seg)) for x in xs]
+    torch.cuda.synchronize()
+    streams, noise, got = [torch.cuda.Stream() for _ in range(3)], torch.randn(2048, 2048, device="cuda"), []
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for i in range(60):
+        with torch.cuda.stream(streams[2]):
+            noise = noise * 0.999
+        with torch.cuda.stream(streams[i % 2]):
+            got.append((api.gated_apply(xs[i % 3], row), api.lora_fwd(xs[i % 3], row, ad, *seg)))
+    torch.cuda.synchronize()
+    for i, (h, y) in enumerate(got):
+        assert torch.equal(h, want[i % 3][0]) and torch.equal(y, want[i % 3][1])
