@@ -29,7 +29,9 @@ __device__ __forceinline__ Rows request_rows(const int* __restrict__ seg_ptr, in
 // The request whose blocks of `span` rows, counted from its first row, include
 // block `w` of the launch: blocks of request s have numbers begin / span + s
 // .. (unique, as ceil(len / span) <= floor(end / span) - floor(begin / span) +
-// 1).  Returns it in *req (-1: none) and its block in *blk.  Block-wide.
+// 1).  Returns it in *req (-1: none) and its block in *blk.  Block-wide.  Where
+// ranges that decrease make several requests claim a block, the last of them has
+// it: the same one in every CTA of a cluster, and a block that it has.
 __device__ __forceinline__ void find_block(const int* __restrict__ seg_ptr, int S, int T, int span, int w, int* sh, int* req,
                                            int* blk) {
   if (threadIdx.x == 0) sh[0] = -1;
@@ -37,11 +39,11 @@ __device__ __forceinline__ void find_block(const int* __restrict__ seg_ptr, int 
   for (int s = threadIdx.x; s < S; s += blockDim.x) {
     const Rows r = request_rows(seg_ptr, s, T);
     const int first = r.begin / span + s, n = (r.end - r.begin + span - 1) / span;
-    if (w >= first && w < first + n) sh[0] = s, sh[1] = w - first;
+    if (w >= first && w < first + n) atomicMax(sh, s);
   }
   __syncthreads();
   *req = sh[0];
-  *blk = sh[1];
+  *blk = sh[0] < 0 ? 0 : w - (request_rows(seg_ptr, sh[0], T).begin / span + sh[0]);
 }
 
 __device__ __forceinline__ int checked_adapter(const int* __restrict__ seg_adapter, int s, int count) {
