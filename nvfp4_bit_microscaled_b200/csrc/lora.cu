@@ -199,6 +199,8 @@ lora_shrink_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
   extern __shared__ uint8_t dyn[];
   allow_next_kernel();
   if (p.after) wait_previous_kernel();
+  // Every CTA waits for the launch before it ends, whatever it finds to do: the
+  // launch after this one waits for this one only, and reads what that one zeroes.
   __shared__ int sh[2];
   __shared__ uint64_t full[kShrinkMaxStages], empty[kShrinkMaxStages], acc_full;
   __shared__ uint32_t tmem_slot;
@@ -214,11 +216,15 @@ lora_shrink_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
     else if (p.E && unit - p.plan_tiles < p.count * p.parts)
       check_finite(p.E, p.elements, p.seg_adapter, p.S, (unit - p.plan_tiles) / p.parts, (unit - p.plan_tiles) % p.parts,
                    p.parts, p.flags, sh);
+    wait_previous_kernel();
     return;
   }
   int s, blk;
   find_block(p.seg_ptr, p.S, p.T, kShrinkRows, item, sh, &s, &blk);
-  if (s < 0) return;
+  if (s < 0) {
+    wait_previous_kernel();
+    return;
+  }
   const int id = checked_adapter(p.seg_adapter, s, p.count);
   const Rows req = request_rows(p.seg_ptr, s, p.T);
   const int t0 = req.begin + blk * kShrinkRows, n = min(kShrinkRows, req.end - t0);
@@ -313,10 +319,8 @@ lora_shrink_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
       if (++stage == p.stages) stage = 0, phase ^= 1u;
     }
     m = __reduce_max_sync(0xFFFFFFFFu, m);
-    if (lane == 0 && m) {
-      wait_previous_kernel();   // *amax is zero
-      atomicMax(p.amax, m << 16);
-    }
+    wait_previous_kernel();   // *amax is zero
+    if (lane == 0 && m) atomicMax(p.amax, m << 16);
   }
   __syncwarp();
   if (warp >= 2) mbar_wait(&acc_full, 0, kErrWaitAccFull);
@@ -388,13 +392,17 @@ __global__ void __launch_bounds__(kRowThreads) lora_shrink_rows_kernel(const uin
     else
       check_finite(p.E, p.elements, p.seg_adapter, p.S, (unit - p.plan_tiles) / p.parts, (unit - p.plan_tiles) % p.parts,
                    p.parts, p.flags, sh);
+    wait_previous_kernel();   // as every block (see above)
     return;
   }
   const int t = blockIdx.x / groups, grp = blockIdx.x - t * groups;
-  if (t >= max(__ldg(p.seg_ptr + p.S), 0)) return;
-  const int id = row_adapter_of(p.seg_ptr, p.seg_adapter, p.S, p.count, t, &row_id);
+  const bool live = t < max(__ldg(p.seg_ptr + p.S), 0);
+  const int id = live ? row_adapter_of(p.seg_ptr, p.seg_adapter, p.S, p.count, t, &row_id) : -1;
   unsigned int* amax = grp == 0 ? p.amax : nullptr;
-  if (id < 0 && !amax) return;
+  if (!live || (id < 0 && !amax)) {
+    wait_previous_kernel();
+    return;
+  }
   const int at = max(id, 0);
   row_low_rank(x + t * ldx, id >= 0 ? A + (static_cast<int64_t>(id) * p.rank + grp * 8) * p.K : nullptr, p.K, p.scale + at,
                p.V + static_cast<int64_t>(t) * p.rank + grp * 8, amax, sums);

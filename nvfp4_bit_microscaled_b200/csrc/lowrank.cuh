@@ -14,7 +14,7 @@ struct RowSums {
 
 // The block's warps split the C columns; v[0 .. 7] = scale * sum_c x[c] a[j][c],
 // summed in warp order.  a == nullptr: no product.  amax != nullptr: max |x|
-// too.  Block-wide.
+// too.  Waits for the launch before (see wait_previous_kernel).  Block-wide.
 __device__ __forceinline__ void row_low_rank(const uint16_t* __restrict__ x, const uint16_t* __restrict__ a, int C,
                                              const float* __restrict__ scale, float* __restrict__ v,
                                              unsigned int* __restrict__ amax, RowSums& sums) {
@@ -57,12 +57,10 @@ __device__ __forceinline__ void row_low_rank(const uint16_t* __restrict__ x, con
       if (w < static_cast<int>(blockDim.x >> 5)) s += sums.v[w][threadIdx.x];
     v[threadIdx.x] = s * __ldg(scale);
   }
+  wait_previous_kernel();   // *amax is zero
   if (amax && threadIdx.x < 32) {
     m = __reduce_max_sync(0xFFFFFFFFu, threadIdx.x < blockDim.x / 32 ? sums.m[threadIdx.x] : 0u);
-    if (threadIdx.x == 0 && m) {
-      wait_previous_kernel();   // *amax is zero
-      atomicMax(amax, m << 16);
-    }
+    if (threadIdx.x == 0 && m) atomicMax(amax, m << 16);
   }
 }
 

@@ -78,3 +78,25 @@ def test_overlapping_ranges_share_numbers_of_blocks(ptr, rows):
         torch.cuda.synchronize()
         assert api.read_device_error(clear=True) == 0
         assert (Y[rows:] == 7.0).all() and (dX[rows:] == 7.0).all() and (V[rows:] == 7.0).all()
+
+
+@pytest.mark.parametrize("rows", [130, 300, 1500])
+@pytest.mark.parametrize("lengths", ["one", "many", "none"])
+def test_zero_batches_after_a_flagged_one(rows, lengths):
+    # a batch of zeros has no maximum to record; the NaN that the batch before left in the same workspace is not its own
+    cin, cout, S = 256, 192, 40
+    row, _ = _copies(synth.weights(cout, cin, 1).cuda())
+    ad = api.LoraAdapters(torch.randn(2, 16, cin).bfloat16().cuda(), torch.randn(2, cout, 16).bfloat16().cuda(),
+                          torch.ones(2, device="cuda"))
+    n = 0 if lengths == "none" else rows
+    at = [min(n, 3 * i) for i in range(S)] + [n] if lengths == "many" else [0] * S + [n]
+    seg, ws = (_i32(at), _i32([i % 3 - 1 for i in range(S)])), api.LoraWorkspace(rows, S, ad, "cuda")
+    full = (_i32([0] * S + [rows]), seg[1])
+    zero, bad = torch.zeros(rows, cin, dtype=torch.bfloat16, device="cuda"), synth.activations(rows, cin, 2).cuda()
+    bad[7, 3] = float("nan")
+    Y, Z = (torch.full((rows, cout), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    for _ in range(20):
+        api.lora_fwd(bad, row, ad, *full, Y=Y, ws=ws)
+        Z.fill_(7.0)
+        api.lora_fwd(zero, row, ad, *seg, Y=Z, ws=ws)
+        assert Y.isnan().all() and (Z[:n] == 0).all() and (Z[n:] == 7.0).all()
