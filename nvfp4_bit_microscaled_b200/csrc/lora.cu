@@ -141,7 +141,7 @@ __device__ void plan_tile(const int* __restrict__ seg_ptr, const int* __restrict
 // (one block for each of `parts` parts of an adapter some request uses).  In a
 // tile that adapters share, the other adapters' rows are zeros in this one's
 // slab, and 0 x NaN would reach them: slab_part keeps such an adapter out.
-__device__ void check_finite(const uint16_t* __restrict__ E, int64_t elements, const int* __restrict__ seg_adapter, int S,
+__device__ void check_finite(const uint16_t* E, int64_t elements, const int* __restrict__ seg_adapter, int S,
                              int id, int part, int parts, int* __restrict__ flags, int* sh) {
   if (threadIdx.x < 2) sh[threadIdx.x] = 0;
   __syncthreads();
@@ -153,7 +153,7 @@ __device__ void check_finite(const uint16_t* __restrict__ E, int64_t elements, c
   const int64_t n8 = elements / 8, lo = n8 * part / parts, hi = n8 * (part + 1) / parts;
   uint32_t m = 0;
 #pragma unroll 8
-  for (int64_t i = lo + threadIdx.x; i < hi; i += blockDim.x) m = max(m, absmax_bits8(__ldg(v + i)));
+  for (int64_t i = lo + threadIdx.x; i < hi; i += blockDim.x) m = max(m, absmax_bits8(v[i]));
   if (m >= 0x7F80u) sh[1] = 1;
   __syncthreads();
   if (threadIdx.x == 0) flags[id * kCheckParts + part] = sh[1];
@@ -378,7 +378,7 @@ lora_shrink_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
 // full one does): a block for each row and eight ranks.  Then the plan's tiles
 // and the checks, as above.
 __global__ void __launch_bounds__(kRowThreads) lora_shrink_rows_kernel(const uint16_t* __restrict__ x, int64_t ldx,
-                                                                       const uint16_t* __restrict__ A,
+                                                                       const uint16_t* A,
                                                                        const __grid_constant__ ShrinkParams p) {
   extern __shared__ uint8_t dyn[];
   __shared__ int sh[2], row_id;
@@ -530,7 +530,7 @@ struct GradSide {
 
 template <int MT>   // tiles of 16 ranks
 __global__ void __launch_bounds__(128)
-lora_grad_kernel(GradSide da, GradSide db, int rank, const int* __restrict__ sorted, const int2* __restrict__ span,
+lora_grad_kernel(GradSide da, GradSide db, int rank, const int* sorted, const int2* span,
                  int slices) {
   constexpr int STAGES = MT == 8 ? 2 : 3;
   constexpr uint32_t Z_TILE = 2 * 64 * 128,   // two halves of 64 columns
@@ -557,7 +557,7 @@ lora_grad_kernel(GradSide da, GradSide db, int rank, const int* __restrict__ sor
   // the rows of four steps, from the one under way on
   __shared__ int rows[4][64];
   auto row_of = [&](int step) {
-    return step < steps && row0(step) + tid < list.y ? __ldg(sorted + list.x + row0(step) + tid) : 0;
+    return step < steps && row0(step) + tid < list.y ? sorted[list.x + row0(step) + tid] : 0;
   };
   if (tid < 64)
 #pragma unroll

@@ -14,8 +14,8 @@ struct RowSums {
 
 // The block's warps split the C columns; v[0 .. 7] = scale * sum_c x[c] a[j][c],
 // summed in warp order.  a == nullptr: no product.  amax != nullptr: max |x|
-// too.  Waits for the launch before (see wait_previous_kernel).  Block-wide.
-__device__ __forceinline__ void row_low_rank(const uint16_t* __restrict__ x, const uint16_t* __restrict__ a, int C,
+// too.  a may come from a launch that this one overlaps.  Waits for the launch before (see wait_previous_kernel).  Block-wide.
+__device__ __forceinline__ void row_low_rank(const uint16_t* __restrict__ x, const uint16_t* a, int C,
                                              const float* __restrict__ scale, float* __restrict__ v,
                                              unsigned int* __restrict__ amax, RowSums& sums) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -27,7 +27,7 @@ __device__ __forceinline__ void row_low_rank(const uint16_t* __restrict__ x, con
     if (!a) continue;
     uint4 av[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) av[j] = __ldg(reinterpret_cast<const uint4*>(a + static_cast<int64_t>(j) * C + c));
+    for (int j = 0; j < 8; ++j) av[j] = *reinterpret_cast<const uint4*>(a + static_cast<int64_t>(j) * C + c);
     const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
 #pragma unroll
     for (int j = 0; j < 8; ++j) {

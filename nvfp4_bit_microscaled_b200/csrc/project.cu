@@ -326,7 +326,7 @@ project_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
     // row r's 16-byte chunk j sits at r * 128 + 16 (j ^ (r % 8)), the 128-byte
     // swizzle that the output maps name.
     const int quarter = warp & 3, half = (warp - EPI_WARP0) >> 2;
-    const float alpha = __fmul_rn(__ldg(p.gsa), __ldg(p.gsb));
+    const float alpha = __fmul_rn(*p.gsa, *p.gsb);
     const uint32_t acc = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + ACC_COL;
     uint8_t* stg = smem + OFF_STG + (warp - EPI_WARP0) * STG_BYTES;
     uint8_t* my_row = stg + lane * 128;

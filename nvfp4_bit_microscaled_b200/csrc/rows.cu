@@ -232,8 +232,8 @@ project_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
         for (int e = 0; e < 4; ++e) {
           const int id = ids[i + e];
           const uint4* b = reinterpret_cast<const uint4*>(p.B + (static_cast<int64_t>(id) * p.N + row0 + ch) * p.rank + k);
-          w[e][0] = id >= 0 && live ? __ldg(b) : make_uint4(0, 0, 0, 0);
-          w[e][1] = id >= 0 && live && k + 8 < p.rank ? __ldg(b + 1) : make_uint4(0, 0, 0, 0);
+          w[e][0] = id >= 0 && live ? *b : make_uint4(0, 0, 0, 0);
+          w[e][1] = id >= 0 && live && k + 8 < p.rank ? b[1] : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -478,7 +478,7 @@ quant_few_rows_kernel(const uint16_t* __restrict__ x, int T, int C, int64_t ld, 
 // rows: 26.1 and 27.4).
 template <int CTAS>
 __global__ void __launch_bounds__(kQuantThreads, 2)
-lora_few_rows_kernel(const uint16_t* __restrict__ x, int T, int C, int64_t ld, QuantOut out, const uint16_t* __restrict__ A,
+lora_few_rows_kernel(const uint16_t* __restrict__ x, int T, int C, int64_t ld, QuantOut out, const uint16_t* A,
                      LoraBatch b, int* __restrict__ row_adapter, float* __restrict__ V) {
   allow_next_kernel();
   if (out.sr) wait_previous_kernel();   // the backward: A comes from the launch before

@@ -107,7 +107,10 @@ cudaError_t launch_after(Kernel kern, unsigned grid, unsigned threads, uint32_t 
 // Device
 // --------------------------------------------------------------------------
 // Programmatic dependent launch: a kernel launched so may start once the one
-// before it allows it, and waits for that one's end (and its memory) here.
+// before it allows it, and waits for that one's end (and its memory) here.  What
+// a launch of the same call writes is read by ordinary loads after the wait, not
+// through the read-only path (__ldg, const __restrict__ parameters): that is for
+// data that stays as it is while the kernel lives, which begins before the wait.
 __device__ __forceinline__ void wait_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void allow_next_kernel() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

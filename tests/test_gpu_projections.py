@@ -100,3 +100,49 @@ def test_zero_batches_after_a_flagged_one(rows, lengths):
         Z.fill_(7.0)
         api.lora_fwd(zero, row, ad, *seg, Y=Z, ws=ws)
         assert Y.isnan().all() and (Z[:n] == 0).all() and (Z[n:] == 7.0).all()
+
+
+@pytest.mark.parametrize("lengths,rank,cin,cout", [([1] * 20, 16, 320, 256), ([60, 40], 128, 192, 256),
+                                                   ([1] * 190, 16, 128, 192), ([150, 3, 200], 32, 1088, 320)])
+def test_adapters_alternate_in_one_workspace(lengths, rank, cin, cout):
+    # what a launch makes for the next ones (transposed adapters, rows of each adapter, the operand's scale) is written
+    # anew in each call of a captured chain: every call gives what it gives alone
+    T, S = sum(lengths), len(lengths)
+    row, col = _copies(synth.weights(cout, cin, 1).cuda())
+    sets = []
+    for i in range(3):
+        g = torch.Generator().manual_seed(i)
+        ad = api.LoraAdapters((torch.randn(130, rank, cin, generator=g) * 0.1).bfloat16().cuda(),
+                              (torch.randn(130, cout, rank, generator=g) * 0.1).bfloat16().cuda(),
+                              (torch.rand(130, generator=g) + 0.5).cuda())
+        seg = (_i32(np.concatenate([[0], np.cumsum(lengths)]).tolist()),
+               torch.randint(-1, 130, (S,), generator=g, dtype=torch.int32).cuda())
+        x, dy = synth.activations(T, cin, 5 + i).cuda(), (synth.gradients(T, cout, 8 + i) * 10.0 ** (2 * i)).cuda()
+        out = dict(Y=torch.zeros(T, cout, dtype=torch.bfloat16, device="cuda"), V=torch.zeros(T, rank, device="cuda"),
+                   dX=torch.zeros(T, cin, dtype=torch.bfloat16, device="cuda"), dA=torch.zeros_like(ad.A), dB=torch.zeros_like(ad.B))
+        sets.append((ad, seg, x, dy, out))
+    spaces = api.LoraWorkspace(T, S, sets[0][0], "cuda"), api.LoraWorkspace(T, S, sets[0][0], "cuda", backward=True)
+
+    def step(ad, seg, x, dy, o):
+        api.lora_fwd(x, row, ad, *seg, Y=o["Y"], V=o["V"], ws=spaces[0])
+        api.lora_bwd(dy, x, o["V"], col, ad, *seg, 3, dX=o["dX"], dA=o["dA"], dB=o["dB"], ws=spaces[1])
+
+    want = []
+    for s in sets:
+        step(*s)
+        torch.cuda.synchronize()
+        want.append({k: v.clone() for k, v in s[4].items()})
+        assert all(v.float().abs().max() > 0 for v in want[-1].values())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for s in sets:
+            step(*s)
+    for _ in range(5):
+        for s in sets:
+            for v in s[4].values():
+                v.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for s, w in zip(sets, want):
+            for k, v in s[4].items():
+                assert torch.equal(v, w[k]), k
