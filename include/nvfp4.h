@@ -319,8 +319,9 @@ nvfp4_status nvfp4_gated_bwd(const void* dH, const void* GU, int64_t T, int64_t 
  * 2^24) may be 0.  Outputs must not overlap inputs.
  *
  * nvfp4_lora_fwd: X's per-tensor amax (over the rows in use) and row copy, the
- *   product with W, and the low-rank product in FP32 on top of it, rounded
- *   once.
+ *   product with W, and the low-rank product on top of it, summed in FP32 and
+ *   rounded once.  V is FP32; in a batch that goes by tiles of rows (more than
+ *   fit the form for few) 16 bits of it enter the product, as two BF16 terms.
  *   W         the weight's row copy (rows = Cout, cols = Cin).
  *   Y         device BF16 [T, Cout], row pitch ldy.
  *   V         NULL, or device FP32 [T, rank] contiguous: scale_i X A_i^T, which

@@ -643,7 +643,7 @@ static LoraLayout lora_layout(int64_t T, int64_t S, int64_t count, int64_t rank,
   L.row_adapter = take(T * 4);
   L.flags = take(slabs ? count * 32 * 4 : 0);
   L.v = take(T * rank * 4);
-  L.slabs = take(slabs * 256 * ((rank + 63) / 64 * 64) * 2);
+  L.slabs = take(slabs * 256 * ((rank + 31) / 32 * 32) * 2 * 2);   // two BF16 terms
   L.data = take(T * (K / 2));
   L.scales = take(pad128(T) * pad4(K / 16));
   L.a_t = take(backward ? count * rank * N * 2 : 0);

@@ -135,7 +135,8 @@ cudaError_t launch_adapter_rows(const FpOperand& x, const FpOperand& w, int64_t 
 // What the adapter tiles read besides the operands, made on the device by
 // lora.cu: the rows in use, for each 256-row tile how many adapters' slabs it
 // has (tile_count) and the first one's index (tile_base), each slab's adapter
-// (`count`: none, zeros), and the slabs, [max_slabs][256][rank padded to 64] BF16.
+// (`count`: none, zeros), and the slabs, [max_slabs][256][ranks / 32, rounded up]
+// [2 terms][32] BF16.
 struct AdapterPlan {
   const int* valid_rows;
   const int* tile_count;
@@ -184,8 +185,8 @@ cudaError_t launch_rows_operand(const void* x, int64_t ldx, int64_t T, int64_t K
                                 float* gs, int num_sms, cudaStream_t s);
 // After the shrink launch: the valid rows' row copy (sr:
 // stochastic rounding) and its decode scale, without scale padding; and with
-// `slabs` (E above) the slabs of the adapter tiles, V / alpha in BF16 with alpha
-// the product's decode scale.
+// `slabs` (E above) the slabs of the adapter tiles, V / alpha as two BF16 terms
+// with alpha the product's decode scale.
 cudaError_t launch_lora_operands(const void* x, int64_t ldx, int64_t T, int64_t K, int sr, uint64_t seed, void* data,
                                  void* scales, float* gs, const float* V, int64_t N, const LoraBatch& b, const LoraPlan& p,
                                  const float* gs_w, bool slabs, int num_sms, cudaStream_t s);

@@ -10,8 +10,8 @@
 // comparing every request's range at once (one round of independent loads).
 // All of it is memory-bound: X and dY are read once by each product, 2 bytes an
 // element for 2 rank operations.
-// V and U are summed in FP32 and kept so; they become BF16, the type of the
-// other operand, only as operands of the second product.
+// V and U are summed in FP32 and kept so; as operands of a BF16 product (tiles
+// of 256 rows, gradients) they are two BF16 terms, 16 bits of the value.
 #include "lowrank.cuh"
 #include "tile.cuh"
 

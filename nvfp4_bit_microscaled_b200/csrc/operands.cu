@@ -50,8 +50,13 @@ __global__ void __launch_bounds__(256) rows_amax_kernel(const uint16_t* __restri
 // stochastic): the arithmetic and the draws of quantize.cu's row kernel, warp
 // item 32 blocks of a row, lane = block.
 //
-// Then slabs: for each adapter that a 256-row tile has rows of, V / alpha in
-// BF16, [256][rank padded to 64], zero in the other rows and past the rank.
+// Then slabs: for each adapter that a 256-row tile has rows of, V / alpha as two
+// BF16 terms (the value rounded, and what that leaves, rounded: 16 bits of it, as
+// one term's 8 would add half of the output's own rounding), zero in the other
+// rows and past the rank.  [256][groups of 32 ranks][2 terms][32].  Up to rank 32
+// the second term costs nothing (a step has room for both); rank 64, 2048 rows of
+// 4096 x 4096 with 32 adapters 54 us with one term and 59 with two, 8192 rows of
+// 8192 x 8192 with eight 276 and 278.
 // alpha = s_gX s_gW: the accumulator the slab is multiplied into is scaled by it
 // at the end.  Eight blocks write a slab, 32 rows each.
 // ---------------------------------------------------------------------------
@@ -70,7 +75,7 @@ struct OperandParams {
   int quant_blocks;
   // slabs
   const float* V;
-  int rank, rank_pad, count, parts;
+  int rank, rank_pad, count, parts;   // rank_pad: a multiple of 32
   const int* tile_count;
   const int* tile_base;
   const int* slab_adapter;
@@ -100,17 +105,23 @@ __device__ void slab_part(const OperandParams& p, int slab, int part, int* sh) {
   for (int u = threadIdx.x; u < 32 * words; u += blockDim.x) {
     const int row = 32 * part + u / words, j = u % words * 8, t = tile * 256 + row;
     const bool own = t < p.T && p.row_adapter[t] == id;
-    uint4 w = make_uint4(0, 0, 0, 0);
+    __nv_bfloat162 hi[4], lo[4];
     if (own && bad) {
-      w = make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
+      *reinterpret_cast<uint4*>(hi) = make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
+      *reinterpret_cast<uint4*>(lo) = make_uint4(0, 0, 0, 0);
     } else if (own && j < p.rank) {
       const float4* v = reinterpret_cast<const float4*>(p.V + static_cast<int64_t>(t) * p.rank + j);
       const float4 a = v[0], b = v[1];
-      __nv_bfloat162 h[4] = {__floats2bfloat162_rn(a.x * inv, a.y * inv), __floats2bfloat162_rn(a.z * inv, a.w * inv),
-                             __floats2bfloat162_rn(b.x * inv, b.y * inv), __floats2bfloat162_rn(b.z * inv, b.w * inv)};
-      w = *reinterpret_cast<uint4*>(h);
+      const float2 z[4] = {make_float2(a.x * inv, a.y * inv), make_float2(a.z * inv, a.w * inv),
+                           make_float2(b.x * inv, b.y * inv), make_float2(b.z * inv, b.w * inv)};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) split_bf16x2(z[k], &hi[k], &lo[k]);
+    } else {
+      *reinterpret_cast<uint4*>(hi) = *reinterpret_cast<uint4*>(lo) = make_uint4(0, 0, 0, 0);
     }
-    *reinterpret_cast<uint4*>(p.slabs + (static_cast<int64_t>(slab) * 256 + row) * p.rank_pad + j) = w;
+    __nv_bfloat16* to = p.slabs + ((static_cast<int64_t>(slab) * 256 + row) * p.rank_pad + (j & ~31)) * 2 + (j & 31);
+    *reinterpret_cast<uint4*>(to) = *reinterpret_cast<uint4*>(hi);
+    *reinterpret_cast<uint4*>(to + 32) = *reinterpret_cast<uint4*>(lo);
   }
 }
 
@@ -258,7 +269,7 @@ cudaError_t launch_lora_operands(const void* x, int64_t ldx, int64_t T, int64_t 
   OperandParams q = rows_params(x, ldx, T, K, p.valid_rows, p.amax, seed, data, scales, gs, num_sms);
   q.V = V;
   q.rank = b.rank;
-  q.rank_pad = (b.rank + 63) / 64 * 64;
+  q.rank_pad = (b.rank + 31) / 32 * 32;
   q.count = b.count;
   q.parts = check_parts(N * b.rank);
   q.tile_count = p.tile_count;

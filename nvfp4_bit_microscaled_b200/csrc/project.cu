@@ -11,8 +11,9 @@
 //            accumulator.  Its first operand, V = scale_i X A_i^T divided by
 //            the FP4 product's decode scale, comes as one 256-row slab for
 //            each adapter that a row tile has rows of, zero in the other rows
-//            (lora.cu builds them), so a tile whose rows use several adapters
-//            adds one K step of 64 for each.
+//            (operands.cu builds them), so a tile whose rows use several adapters
+//            adds K steps for each: one for every 32 ranks, whose 64 columns of
+//            the slab are V's two BF16 terms, both by the same 32 ranks of B.
 //
 // The pipeline: a cluster of two CTAs computes a 256 x 256 accumulator tile,
 // persistent, 16 warps in four groups:
@@ -76,7 +77,7 @@ struct Params {
   const int* tile_base;
   const int* slab_adapter;
   const int* valid_rows;
-  int rank_blocks;      // K steps of 64 for each slab
+  int rank, rank_blocks;   // K steps for each slab: 32 ranks each
   __nv_bfloat16* Y;
   int64_t ldy;
 };
@@ -195,7 +196,7 @@ project_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
               if (!mbar_wait(&empty[stage], phase ^ 1u, kErrWaitEmpty)) { ok = false; break; }
               if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * (A_BYTES + B_BYTES));
               tma_load_2d_pair(smem + OFF_A + stage * A_BYTES, &tmE, full_l + stage * 8, 64 * rb, row_v);
-              tma_load_2d_pair(smem + OFF_B + stage * B_BYTES, &tmF, full_l + stage * 8, 64 * rb, row_ad);
+              tma_load_2d_pair(smem + OFF_B + stage * B_BYTES, &tmF, full_l + stage * 8, 32 * rb, row_ad);
               mbar_arrive(&sfd_full[stage]);   // no scales in this step
               issued |= 1u << stage;
               issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
@@ -251,16 +252,23 @@ project_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
           // only MMAs of one kind are ordered among themselves: the FP4 steps
           // finish before a BF16 step adds to the same accumulator
           tc_commit_pair(kind_done);
-          ok = mbar_wait(kind_done, kind_phase, kErrWaitAccFull);
+          if (!mbar_wait(kind_done, kind_phase, kErrWaitAccFull)) { *abort_flag = 1; break; }
           kind_phase ^= 1u;
           tc_fence_after();
-          for (int e = 0; e < count && ok; ++e) {
+          int ranks = p.rank;   // left of the slab under way
+          for (int e = 0; e < count; ++e) {
             if (!mbar_wait_cluster(&sf_full[stage], phase, kErrWaitFull)) { ok = false; break; }
             tc_fence_after();
             const uint64_t adesc = adesc0 + static_cast<uint64_t>(stage * (A_BYTES >> 4));
             const uint64_t bdesc = bdesc0 + static_cast<uint64_t>(stage * (B_BYTES >> 4));
-#pragma unroll
-            for (int kb = 0; kb < 4; ++kb) mma_bf16_pair(tmem + ACC_COL, adesc + 2 * kb, bdesc + 2 * kb, IDESC_BF16, 1);
+            // columns 0-31 of the slab's step: first terms, 32-63: second (4 x 16 bytes on); 16 ranks an MMA
+            mma_bf16_pair(tmem + ACC_COL, adesc, bdesc, IDESC_BF16, 1);
+            mma_bf16_pair(tmem + ACC_COL, adesc + 4, bdesc, IDESC_BF16, 1);
+            if (ranks > 16) {
+              mma_bf16_pair(tmem + ACC_COL, adesc + 2, bdesc + 2, IDESC_BF16, 1);
+              mma_bf16_pair(tmem + ACC_COL, adesc + 6, bdesc + 2, IDESC_BF16, 1);
+            }
+            if ((ranks -= 32) <= 0) ranks = p.rank;
             tc_commit_pair_mc(&empty[stage], 0x3);
             if (++stage == STAGES) stage = 0, phase ^= 1u;
           }
@@ -500,10 +508,10 @@ cudaError_t launch_gated_tiles(const FpOperand& a, const FpOperand& w, int64_t M
 cudaError_t launch_adapter_tiles(const FpOperand& a, const FpOperand& w, int64_t M, int64_t N, int64_t K,
                                  const AdapterPlan& plan, const void* adapter_rows, int64_t adapters, int64_t rank,
                                  void* Y, int64_t ldy, int num_sms, cudaStream_t s) {
-  const int64_t rank_pad = (rank + 63) / 64 * 64;
+  const int64_t rank_blocks = (rank + 31) / 32;
   CUtensorMap tmA, tmB, tmD, tmE, tmF;
   if (!operand_map(&tmA, a.data, M, K, 128) || !operand_map(&tmB, w.data, N, K, 128) ||
-      !bf16_map(&tmD, Y, M, N, ldy, 32) || !bf16_map(&tmE, plan.slabs, plan.max_slabs * 256, rank_pad, rank_pad, 128) ||
+      !bf16_map(&tmD, Y, M, N, ldy, 32) || !bf16_map(&tmE, plan.slabs, plan.max_slabs * 256, rank_blocks * 64, rank_blocks * 64, 128) ||
       !bf16_map(&tmF, adapter_rows, adapters * N, rank, rank, 128))
     return cudaErrorInvalidValue;
   Params p = {};
@@ -518,7 +526,8 @@ cudaError_t launch_adapter_tiles(const FpOperand& a, const FpOperand& w, int64_t
   p.tile_base = plan.tile_base;
   p.slab_adapter = plan.slab_adapter;
   p.valid_rows = plan.valid_rows;
-  p.rank_blocks = static_cast<int>(rank_pad / 64);
+  p.rank = static_cast<int>(rank);
+  p.rank_blocks = static_cast<int>(rank_blocks);
   p.Y = static_cast<__nv_bfloat16*>(Y);
   p.ldy = ldy;
   const int64_t tiles = ((M + 255) / 256) * ((N + 255) / 256);

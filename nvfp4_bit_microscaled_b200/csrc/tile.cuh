@@ -138,6 +138,14 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64
       : "memory");
 }
 
+// Two FP32 values as a BF16 term and the BF16 rounding of what it leaves (an
+// infinity leaves nothing).
+__device__ __forceinline__ void split_bf16x2(float2 v, __nv_bfloat162* hi, __nv_bfloat162* lo) {
+  *hi = __floats2bfloat162_rn(v.x, v.y);
+  const float2 h = __bfloat1622float2(*hi);
+  *lo = __floats2bfloat162_rn(fabsf(h.x) == INFINITY ? 0.0f : v.x - h.x, fabsf(h.y) == INFINITY ? 0.0f : v.y - h.y);
+}
+
 template <int N>
 __device__ __forceinline__ void regs_release() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));

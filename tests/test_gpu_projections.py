@@ -6,6 +6,7 @@ import torch
 
 from nvfp4_bit_microscaled_b200 import api, synth
 from tests import _nvfp4_ref as R
+from tests import test_gpu_lora as G
 
 pytestmark = pytest.mark.gpu
 
@@ -146,3 +147,43 @@ def test_adapters_alternate_in_one_workspace(lengths, rank, cin, cout):
         for s, w in zip(sets, want):
             for k, v in s[4].items():
                 assert torch.equal(v, w[k]), k
+
+
+def _projected(b, x, first, second, codes, weight, terms):
+    """Wanted rows and their bound: the quantized product (FP32 accumulation), the low-rank product of V in `terms`
+    roundings' accuracy (FP32 accumulation, V's own FP32 sum), one rounding to BF16."""
+    n = b["n"]
+    _, va, low, la = G._low_rank(b, x, first, second)
+    lva = np.zeros_like(low)
+    for lo, hi, i in zip(b["ptr"], b["ptr"][1:], b["ids"]):
+        if 0 <= i < b["count"]:
+            lva[lo:hi] = va[lo:hi] @ np.abs(second[i]).T
+    want = codes @ weight.T + low[:n]
+    tol = R.GEMM_REL * (np.abs(codes) @ np.abs(weight).T) + (terms + R.GEMM_REL) * la[:n] + G.F32_SUM * lva[:n]
+    return want, tol + R.BF16 * (np.abs(want) + tol)
+
+
+# V is summed in FP32.  Few rows keep it so; the tiles take it as two BF16 terms, the second a rounding of what the
+# first leaves: 2^-8 of 2^-8
+TERMS = 2.0 ** -16
+
+
+@pytest.mark.parametrize("zero_weight", [False, True])
+@pytest.mark.parametrize("case", [2, 4, 5, 8, 9, 10, 11, 14, 16, 17, 20, 23])
+def test_the_low_rank_product_is_rounded_once(case, zero_weight):
+    b = G._make(*G.CASES[case], seed=40 + case)
+    n, cin, cout = b["n"], b["cin"], b["cout"]
+    if zero_weight:
+        b["row"], b["col"] = _copies(torch.zeros(cout, cin, dtype=torch.bfloat16, device="cuda"))
+    x, dy = R.f64(b["x"][:, :cin]), R.f64(b["dy"][:, :cout])
+    x[n:], dy[n:] = 0, 0
+    A, B = R.f64(b["A"]), R.f64(b["B"])
+    V = torch.zeros(b["T"], b["rank"], device="cuda")
+    Y = api.lora_fwd(b["X"], b["row"], b["ad"], *b["seg"], V=V)
+    codes = R.decode_bf16(b["x"][:n, :cin].contiguous(), "row")
+    want, tol = _projected(b, x, A, B, codes, R.decode(b["row"]), TERMS)
+    R.assert_within(R.f64(Y)[:n], want, tol, "Y")
+    dX, _, _ = api.lora_bwd(b["dY"], b["X"], V, b["col"], b["ad"], *b["seg"], 5)
+    codes = R.decode_bf16(b["dy"][:n, :cout].contiguous(), "row", sr=True, seed=5)
+    want, tol = _projected(b, dy, B.transpose(0, 2, 1), A.transpose(0, 2, 1), codes, R.decode(b["col"]), TERMS)
+    R.assert_within(R.f64(dX)[:n], want, tol, "dX")
