@@ -610,7 +610,7 @@ nvfp4_status nvfp4_gated_bwd(const void* dH, const void* GU, int64_t T, int64_t 
 // Workspace of the adapter calls: scalars, plan, V or U, slabs, the operand's
 // row copy and, for the backward, the transposed adapters and the lists of rows.
 struct LoraLayout {
-  size_t tile_count, tile_base, slab_adapter, slab_source, row_adapter, flags, v, slabs, data, scales, a_t, b_t, sorted, span, total;
+  size_t tile_count, tile_base, slab_adapter, slab_source, row_adapter, tile_direct, second_max, v, slabs, data, scales, a_t, b_t, sorted, span, total;
 };
 // Few rows and ranks: the kernel that streams W and adds the low-rank products
 // row by row, 16 ranks at a time, each CTA of a tile those of its share of the
@@ -641,7 +641,8 @@ static LoraLayout lora_layout(int64_t T, int64_t S, int64_t count, int64_t rank,
   L.slab_adapter = take(slabs * 4);
   L.slab_source = take(slabs * 4);
   L.row_adapter = take(T * 4);
-  L.flags = take(slabs ? count * 32 * 4 : 0);
+  L.tile_direct = take(tiles * 4);
+  L.second_max = take(slabs ? count * 32 * 4 : 0);
   L.v = take(T * rank * 4);
   L.slabs = take(slabs * 256 * ((rank + 31) / 32 * 32) * 2 * 2);   // two BF16 terms
   L.data = take(T * (K / 2));
@@ -713,7 +714,8 @@ static nvfp4_status lora_project(const void* x, int64_t T, int64_t ldx, const nv
   plan.slab_adapter = reinterpret_cast<int*>(ws + L.slab_adapter);
   plan.slab_source = reinterpret_cast<int*>(ws + L.slab_source);
   plan.row_adapter = reinterpret_cast<int*>(ws + L.row_adapter);
-  plan.flags = reinterpret_cast<int*>(ws + L.flags);
+  plan.tile_direct = reinterpret_cast<int*>(ws + L.tile_direct);
+  plan.second_max = reinterpret_cast<int*>(ws + L.second_max);
   plan.slabs = ws + L.slabs;
   plan.amax = scalars;
   const FpOperand xq{ws + L.data, ws + L.scales, scalars + 1};
@@ -763,7 +765,7 @@ static nvfp4_status lora_project(const void* x, int64_t T, int64_t ldx, const nv
   }
   if (by_rows) return beside ? join(&f) : cuda_status(gradients(s));
   AdapterPlan ap{plan.valid_rows, plan.tile_count, plan.tile_base, plan.slab_source, plan.slabs,
-                 b.S + (T + 255) / 256};
+                 b.S + (T + 255) / 256, plan.tile_direct, v, plan.row_adapter};
   e = launch_adapter_tiles(xq, operand(W), T, N, K, ap, expand, b.count, b.rank, out, ldo, sms, s);
   if (e != cudaSuccess) return fail(&f, cuda_status(e));
   if (beside) return join(&f);

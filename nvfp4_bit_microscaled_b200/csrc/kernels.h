@@ -144,6 +144,11 @@ struct AdapterPlan {
   const int* slab_adapter;
   const void* slabs;
   int64_t max_slabs;
+  // Tiles whose slabs cannot hold V / alpha (tile_direct not 0) take V [T, rank]
+  // FP32 itself, by each row's adapter (-1 or -2: none).
+  const int* tile_direct;
+  const float* V;
+  const int* row_adapter;
 };
 
 // Y = A W^T + (slabs) (adapter rows)^T, tiles of 256 rows; adapter_rows
@@ -160,19 +165,20 @@ struct LoraPlan {
   int* slab_adapter;   // per slab: its adapter
   int* slab_source;    // the same, `count` where the adapter is kept out (written with the slabs)
   int* row_adapter;    // per row: adapter, -1 none, -2 padding
-  int* flags;          // per adapter, 32 parts: second operand not finite
+  int* tile_direct;    // per 256-row tile: low-rank products in the epilogue (written with the slabs)
+  int* second_max;     // per adapter, 32 parts: largest magnitude of the second operand, BF16 bits
   void* slabs;
   float* amax;         // max |x| over the requests' rows
 };
 
 // V[t, :] = scale_i x[t, :] A_i^T (A [count, rank, K] BF16) for rows of requests
-// with an adapter, the plan, and *p.amax (zeroed: it is 0 already).  E: NULL, or the second operands ([count, N, rank]) of slabs to
-// come, to be checked for values that are not finite.
+// with an adapter, the plan, and *p.amax (zeroed: it is 0 already).  E: NULL, or
+// the second operands ([count, N, rank]) of slabs to come, whose maxima are taken.
 cudaError_t launch_lora_shrink(const void* x, int64_t ldx, int64_t T, int64_t K, const void* A, const void* E, int64_t N,
                                const LoraBatch& b, const LoraPlan& p, bool zeroed, float* V, int num_sms,
                                cudaStream_t s);
 // Parts in which an adapter's second operand is checked (of about 64 KB), at
-// most kCheckParts, the pitch of the flags.
+// most kCheckParts, the pitch of the maxima.
 constexpr int kCheckParts = 32;
 inline int check_parts(int64_t elements) {
   const int64_t n = (elements * 2 + 65535) / 65536;

@@ -85,6 +85,7 @@ struct PlanOut {
   int* valid_rows;
   int* tile_count;
   int* tile_base;
+  int* tile_direct;
   int* slab_adapter;   // or null: no slabs to come
   int* row_adapter;
 };
@@ -133,16 +134,17 @@ __device__ void plan_tile(const int* __restrict__ seg_ptr, const int* __restrict
     if (threadIdx.x == 0) {
       out.tile_base[tile] = base;
       out.tile_count[tile] = n;
+      out.tile_direct[tile] = 0;   // slab_part may set it
     }
   }
 }
 
-// Whether the second operand of an adapter holds a value that is not finite
-// (one block for each of `parts` parts of an adapter some request uses).  In a
-// tile that adapters share, the other adapters' rows are zeros in this one's
-// slab, and 0 x NaN would reach them: slab_part keeps such an adapter out.
-__device__ void check_finite(const uint16_t* E, int64_t elements, const int* __restrict__ seg_adapter, int S,
-                             int id, int part, int parts, int* __restrict__ flags, int* sh) {
+// The largest magnitude (BF16 bits) in the second operand of an adapter, one
+// block for each of `parts` parts of an adapter some request uses.  Where it is
+// not finite slab_part keeps the adapter out: in a tile that adapters share, the
+// other adapters' rows are zeros in this one's slab, and 0 x NaN would reach them.
+__device__ void second_maximum(const uint16_t* E, int64_t elements, const int* __restrict__ seg_adapter, int S,
+                               int id, int part, int parts, int* __restrict__ second_max, int* sh) {
   if (threadIdx.x < 2) sh[threadIdx.x] = 0;
   __syncthreads();
   for (int s = threadIdx.x; s < S; s += blockDim.x)
@@ -154,9 +156,10 @@ __device__ void check_finite(const uint16_t* E, int64_t elements, const int* __r
   uint32_t m = 0;
 #pragma unroll 8
   for (int64_t i = lo + threadIdx.x; i < hi; i += blockDim.x) m = max(m, absmax_bits8(v[i]));
-  if (m >= 0x7F80u) sh[1] = 1;
+  m = __reduce_max_sync(0xFFFFFFFFu, m);
+  if ((threadIdx.x & 31) == 0) atomicMax(&sh[1], static_cast<int>(m));
   __syncthreads();
-  if (threadIdx.x == 0) flags[id * kCheckParts + part] = sh[1];
+  if (threadIdx.x == 0) second_max[id * kCheckParts + part] = sh[1];
 }
 
 // ---------------------------------------------------------------------------
@@ -183,10 +186,10 @@ struct ShrinkParams {
   const int* seg_ptr;
   const int* seg_adapter;
   PlanOut plan;
-  const uint16_t* E;     // second operands to be checked, or null
+  const uint16_t* E;     // second operands whose maxima are taken, or null
   int64_t elements;
   int parts;
-  int* flags;
+  int* second_max;
   unsigned int* amax;
   float* V;
   bool after;   // A comes from the launch before
@@ -214,8 +217,8 @@ lora_shrink_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
     if (unit < p.plan_tiles)
       plan_tile(p.seg_ptr, p.seg_adapter, p.S, p.T, p.count, unit, p.plan, reinterpret_cast<uint32_t*>(dyn), sh);
     else if (p.E && unit - p.plan_tiles < p.count * p.parts)
-      check_finite(p.E, p.elements, p.seg_adapter, p.S, (unit - p.plan_tiles) / p.parts, (unit - p.plan_tiles) % p.parts,
-                   p.parts, p.flags, sh);
+      second_maximum(p.E, p.elements, p.seg_adapter, p.S, (unit - p.plan_tiles) / p.parts, (unit - p.plan_tiles) % p.parts,
+                   p.parts, p.second_max, sh);
     wait_previous_kernel();
     return;
   }
@@ -390,8 +393,8 @@ __global__ void __launch_bounds__(kRowThreads) lora_shrink_rows_kernel(const uin
     if (unit < p.plan_tiles)
       plan_tile(p.seg_ptr, p.seg_adapter, p.S, p.T, p.count, unit, p.plan, reinterpret_cast<uint32_t*>(dyn), sh);
     else
-      check_finite(p.E, p.elements, p.seg_adapter, p.S, (unit - p.plan_tiles) / p.parts, (unit - p.plan_tiles) % p.parts,
-                   p.parts, p.flags, sh);
+      second_maximum(p.E, p.elements, p.seg_adapter, p.S, (unit - p.plan_tiles) / p.parts, (unit - p.plan_tiles) % p.parts,
+                   p.parts, p.second_max, sh);
     wait_previous_kernel();   // as every block (see above)
     return;
   }
@@ -774,11 +777,11 @@ cudaError_t launch_lora_shrink(const void* x, int64_t ldx, int64_t T, int64_t K,
   q.scale = b.scale;
   q.seg_ptr = b.seg_ptr;
   q.seg_adapter = b.seg_adapter;
-  q.plan = PlanOut{p.valid_rows, p.tile_count, p.tile_base, E ? p.slab_adapter : nullptr, p.row_adapter};
+  q.plan = PlanOut{p.valid_rows, p.tile_count, p.tile_base, p.tile_direct, E ? p.slab_adapter : nullptr, p.row_adapter};
   q.E = static_cast<const uint16_t*>(E);
   q.elements = N * b.rank;
   q.parts = check_parts(q.elements);
-  q.flags = p.flags;
+  q.second_max = p.second_max;
   q.amax = amax;
   q.V = V;
   q.after = zeroed;

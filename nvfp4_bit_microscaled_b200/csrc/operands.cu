@@ -58,7 +58,9 @@ __global__ void __launch_bounds__(256) rows_amax_kernel(const uint16_t* __restri
 // 4096 x 4096 with 32 adapters 54 us with one term and 59 with two, 8192 rows of
 // 8192 x 8192 with eight 276 and 278.
 // alpha = s_gX s_gW: the accumulator the slab is multiplied into is scaled by it
-// at the end.  Eight blocks write a slab, 32 rows each.
+// at the end.  Eight blocks write a slab, 32 rows each.  Where a finite V / alpha
+// or its products would leave FP32's range (alpha may be a subnormal, or zero),
+// the tile is marked: its epilogue adds V's products itself, after alpha.
 // ---------------------------------------------------------------------------
 struct OperandParams {
   const uint16_t* x;
@@ -80,7 +82,8 @@ struct OperandParams {
   const int* tile_base;
   const int* slab_adapter;
   const int* row_adapter;
-  const int* flags;
+  int* tile_direct;
+  const int* second_max;
   const float* gs_w;
   int* slab_source;
   __nv_bfloat16* slabs;
@@ -95,12 +98,21 @@ __device__ void slab_part(const OperandParams& p, int slab, int part, int* sh) {
   const int tile = sh[0];
   if (tile < 0) return;
   const int id = p.slab_adapter[slab];
+  if (threadIdx.x < 32) {
+    const int m = threadIdx.x < p.parts ? p.second_max[id * kCheckParts + threadIdx.x] : 0;
+    const int most = __reduce_max_sync(0xFFFFFFFFu, m);
+    if (threadIdx.x == 0) sh[1] = most;
+  }
+  __syncthreads();
   // an adapter with a value that is not finite: NaN for its own rows, and an
   // index past the adapters, whose rows the tile's loads fill with zeros
-  const int bad = __syncthreads_or(threadIdx.x < p.parts && p.flags[id * kCheckParts + threadIdx.x]);
+  const bool bad = sh[1] >= 0x7F80;
   if (part == 0 && threadIdx.x == 0) p.slab_source[slab] = bad ? p.count : id;
-  // a scale that is zero or not finite: V / alpha keeps NaN and infinity, as the product it joins
-  const float inv = __fdiv_rn(1.0f, __fmul_rn(decode_scale(*p.amax), __ldg(p.gs_w)));
+  const float alpha = __fmul_rn(decode_scale(*p.amax), __ldg(p.gs_w)), inv = __fdiv_rn(1.0f, alpha);
+  const float second = bf16_bits_to_f32(sh[1]);
+  bool over = false;
+  // up to 128 products and the FP4 sum (below 2^48) stay below 2^104
+  auto leaves = [&](float v, float z) { return isfinite(v) && !(fabsf(z) < 0x1p127f && fabsf(z) * second < 0x1p96f); };
   const int words = p.rank_pad / 8;
   for (int u = threadIdx.x; u < 32 * words; u += blockDim.x) {
     const int row = 32 * part + u / words, j = u % words * 8, t = tile * 256 + row;
@@ -114,8 +126,12 @@ __device__ void slab_part(const OperandParams& p, int slab, int part, int* sh) {
       const float4 a = v[0], b = v[1];
       const float2 z[4] = {make_float2(a.x * inv, a.y * inv), make_float2(a.z * inv, a.w * inv),
                            make_float2(b.x * inv, b.y * inv), make_float2(b.z * inv, b.w * inv)};
+      const float2 from[4] = {make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)};
 #pragma unroll
-      for (int k = 0; k < 4; ++k) split_bf16x2(z[k], &hi[k], &lo[k]);
+      for (int k = 0; k < 4; ++k) {
+        split_bf16x2(z[k], &hi[k], &lo[k]);
+        over = over || leaves(from[k].x, z[k].x) || leaves(from[k].y, z[k].y);
+      }
     } else {
       *reinterpret_cast<uint4*>(hi) = *reinterpret_cast<uint4*>(lo) = make_uint4(0, 0, 0, 0);
     }
@@ -123,6 +139,8 @@ __device__ void slab_part(const OperandParams& p, int slab, int part, int* sh) {
     *reinterpret_cast<uint4*>(to) = *reinterpret_cast<uint4*>(hi);
     *reinterpret_cast<uint4*>(to + 32) = *reinterpret_cast<uint4*>(lo);
   }
+  // (a scale that is not finite flags the whole batch: NaN whatever is added)
+  if (__syncthreads_or(over && isfinite(alpha)) && threadIdx.x == 0) p.tile_direct[tile] = 1;
 }
 
 // NARROW: every block counter (element index / 16) fits in 32 bits.
@@ -276,7 +294,8 @@ cudaError_t launch_lora_operands(const void* x, int64_t ldx, int64_t T, int64_t 
   q.tile_base = p.tile_base;
   q.slab_adapter = p.slab_adapter;
   q.row_adapter = p.row_adapter;
-  q.flags = p.flags;
+  q.tile_direct = p.tile_direct;
+  q.second_max = p.second_max;
   q.gs_w = gs_w;
   q.slab_source = p.slab_source;
   q.slabs = static_cast<__nv_bfloat16*>(p.slabs);

@@ -14,6 +14,10 @@
 //            (operands.cu builds them), so a tile whose rows use several adapters
 //            adds K steps for each: one for every 32 ranks, whose 64 columns of
 //            the slab are V's two BF16 terms, both by the same 32 ranks of B.
+//            Where V over the decode scale leaves FP32's range, a tile has no
+//            such steps: its epilogue adds V's products in FP32 (slow, and rare:
+//            scales whose product is next to nothing, adapters out of all
+//            proportion to W).
 //
 // The pipeline: a cluster of two CTAs computes a 256 x 256 accumulator tile,
 // persistent, 16 warps in four groups:
@@ -78,6 +82,10 @@ struct Params {
   const int* slab_adapter;
   const int* valid_rows;
   int rank, rank_blocks;   // K steps for each slab: 32 ranks each
+  const int* tile_direct;
+  const float* V;
+  const int* row_adapter;
+  const __nv_bfloat16* B;
   __nv_bfloat16* Y;
   int64_t ldy;
 };
@@ -92,6 +100,45 @@ __device__ __forceinline__ void tile_at(int t, int num_m, int num_n, int group_m
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
+}
+
+// ADAPTER: slabs that row tile tm adds to its accumulator.
+__device__ __forceinline__ int tile_slabs(const Params& p, int tm) { return p.tile_direct[tm] ? 0 : p.tile_count[tm]; }
+
+// ADAPTER, a tile without slabs: 128 columns of 32 rows, y = alpha acc + V B^T
+// in FP32, eight columns at a time.  Warp-wide.
+__device__ __noinline__ void direct_tile(const Params& p, uint32_t acc, float alpha, int row, int M, int col0) {
+  const int id = row < M ? p.row_adapter[row] : -1;
+  const float* v = p.V + static_cast<int64_t>(row) * p.rank;
+#pragma unroll 1
+  for (int c = 0; c < 128; c += 8) {
+    uint32_t r[8];
+    tmem_ld_32x32b_x8(acc + c, r);
+    tmem_ld_wait();
+    const int col = col0 + c;
+    if (row < M && col < p.N) {
+      float low[8] = {};
+      const __nv_bfloat16* b = p.B + (static_cast<int64_t>(id) * p.N + col) * p.rank;
+#pragma unroll 1
+      for (int j = 0; id >= 0 && j < p.rank; j += 8) {
+        const float4 v0 = *reinterpret_cast<const float4*>(v + j), v1 = *reinterpret_cast<const float4*>(v + j + 4);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint4 w = *reinterpret_cast<const uint4*>(b + e * p.rank + j);
+          const float2 w0 = bf16x2_to_f32x2(w.x), w1 = bf16x2_to_f32x2(w.y), w2 = bf16x2_to_f32x2(w.z),
+                       w3 = bf16x2_to_f32x2(w.w);
+          low[e] = __fmaf_rn(v0.y, w0.y, __fmaf_rn(v0.x, w0.x, low[e]));
+          low[e] = __fmaf_rn(v0.w, w1.y, __fmaf_rn(v0.z, w1.x, low[e]));
+          low[e] = __fmaf_rn(v1.y, w2.y, __fmaf_rn(v1.x, w2.x, low[e]));
+          low[e] = __fmaf_rn(v1.w, w3.y, __fmaf_rn(v1.z, w3.x, low[e]));
+        }
+      }
+      auto y = [&](int e) { return __fmaf_rn(__uint_as_float(r[e]), alpha, low[e]); };
+      *reinterpret_cast<uint4*>(p.Y + static_cast<int64_t>(row) * p.ldy + col) =
+          make_uint4(pack_bf16(y(0), y(1)), pack_bf16(y(2), y(3)), pack_bf16(y(4), y(5)), pack_bf16(y(6), y(7)));
+    }
+    __syncwarp();
+  }
 }
 
 template <int KIND, int ACT>
@@ -188,7 +235,7 @@ project_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
           if (++stage == STAGES) stage = 0, phase ^= 1u;
         }
         if (KIND == kAdapter && ok) {
-          const int count = p.tile_count[tm], base = p.tile_base[tm];
+          const int count = tile_slabs(p, tm), base = p.tile_base[tm];
           for (int e = 0; e < count && ok; ++e) {
             const int row_v = (base + e) * 256 + 128 * static_cast<int>(rank);
             const int row_ad = p.slab_adapter[base + e] * p.N + row_b;
@@ -223,7 +270,7 @@ project_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
         if (KIND == kAdapter) {
           int tm, tn;
           tile_at(t, num_m, num_n, p.group_m, &tm, &tn);
-          count = p.tile_count[tm] * p.rank_blocks;
+          count = tile_slabs(p, tm) * p.rank_blocks;
         }
         if (!mbar_wait_cluster(acc_empty, acc_phase ^ 1u, kErrWaitAccEmpty)) { *abort_flag = 1; break; }
         tc_fence_after();
@@ -291,7 +338,7 @@ project_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
       tile_at(t, num_m, num_n, p.group_m, &tm, &tn);
       const bool a_sf = 2 * tm + static_cast<int>(rank) < sf_rows_a;
       const bool b_sf0 = KIND == kGated || 2 * tn < sf_rows_b, b_sf1 = KIND == kGated || 2 * tn + 1 < sf_rows_b;
-      const int extra = KIND == kAdapter ? p.tile_count[tm] * p.rank_blocks : 0;
+      const int extra = KIND == kAdapter ? tile_slabs(p, tm) * p.rank_blocks : 0;
       bool ok = true;
       for (int kt = 0; kt < num_kt + extra; ++kt) {
         if (!mbar_wait(&sfd_full[stage], phase, kErrWaitFull) ||
@@ -357,6 +404,7 @@ project_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
     for (int t = pair; t < num_tiles && !*abort_flag; t += num_pairs) {
       int tm, tn;
       tile_at(t, num_m, num_n, p.group_m, &tm, &tn);
+      const bool direct = KIND == kAdapter && p.tile_direct[tm];
       if (!mbar_wait_cluster(acc_full, acc_phase, kErrWaitAccFull)) { *abort_flag = 1; break; }
       acc_phase ^= 1u;
       tc_fence_after();
@@ -398,6 +446,11 @@ project_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
           });
           if (row0 + lane < M) run_max = fmaxf(run_max, tile_max);
         }
+      } else if (direct) {
+        direct_tile(p, acc + 128 * half, alpha, row0 + lane, M, tn * 256 + 128 * half);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(acc_empty_l);
       } else {
         uint32_t w[2][32];
 #pragma unroll
@@ -527,6 +580,10 @@ cudaError_t launch_adapter_tiles(const FpOperand& a, const FpOperand& w, int64_t
   p.slab_adapter = plan.slab_adapter;
   p.valid_rows = plan.valid_rows;
   p.rank = static_cast<int>(rank);
+  p.tile_direct = plan.tile_direct;
+  p.V = plan.V;
+  p.row_adapter = plan.row_adapter;
+  p.B = static_cast<const __nv_bfloat16*>(adapter_rows);
   p.rank_blocks = static_cast<int>(rank_blocks);
   p.Y = static_cast<__nv_bfloat16*>(Y);
   p.ldy = ldy;

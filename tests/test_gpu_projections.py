@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 import torch
 
+import oracle as O
 from nvfp4_bit_microscaled_b200 import api, synth
 from tests import _nvfp4_ref as R
 from tests import test_gpu_lora as G
@@ -187,3 +188,59 @@ def test_the_low_rank_product_is_rounded_once(case, zero_weight):
     codes = R.decode_bf16(b["dy"][:n, :cout].contiguous(), "row", sr=True, seed=5)
     want, tol = _projected(b, dy, B.transpose(0, 2, 1), A.transpose(0, 2, 1), codes, R.decode(b["col"]), TERMS)
     R.assert_within(R.f64(dX)[:n], want, tol, "dX")
+
+
+EXTREMES = {   # scales of x (or dy), w, the last adapter's scale, its B (forward) or A (backward)
+    "product 1e-34": (1e-17, 1e-17, 1.0, 1.0),
+    "product 1e-38": (1e-19, 1e-19, 1.0, 1.0),
+    "decode scale 0": (1e-24, 1e-25, 1.0, 1.0),
+    "subnormal scale": (1.0, 2e-34, 1.0, 1.0),   # 2688 / max|W| is finite, the decode scale max|W| / 2688 no normal number
+    "large adapter": (1.0, 1.0, 3e33, 1.0),
+    "large by small": (1.0, 1.0, 3e35, 1e-33),
+}
+
+
+@pytest.mark.parametrize("name", EXTREMES)
+@pytest.mark.parametrize("lengths,ids,cin,cout,rank,count,pad", [
+    ([129], [0], 128, 64, 16, 1, 0),
+    ([300, 1, 0, 211], [1, 0, 1, -1], 576, 320, 128, 2, 17),
+    ([200, 56, 300, 3], [0, 0, 1, -1], 192, 832, 40, 2, 4),      # the last adapter in the later tiles only
+    ([70], [0], 128, 192, 128, 1, 3),
+    ([1] * 190, [i % 131 - 1 for i in range(190)], 128, 192, 8, 130, 0),
+])
+def test_low_rank_sums_where_the_decode_scale_is_small(name, lengths, ids, cin, cout, rank, count, pad):
+    # V divided by the quantized product's decode scale leaves FP32's range although every output is inside it
+    sx, sw, ss, se = EXTREMES[name]
+    b = G._make(lengths, ids, cin, cout, rank, count, pad, seed=len(lengths))
+    n = b["n"]
+    b["x"], b["dy"] = (b["x"].float() * sx).bfloat16(), (b["dy"].float() * sx).bfloat16()
+    b["scale"][-1] *= ss
+    w = (b["w"].float() * sw).bfloat16().cuda()
+    row, col = _copies(w)
+    V = torch.zeros(b["T"], rank, device="cuda")
+    for forward in (True, False):
+        A, B = b["A"].clone(), b["B"].clone()
+        (B if forward else A)[-1] *= se
+        ad = api.LoraAdapters(A.cuda(), B.cuda(), b["scale"].cuda())
+        A, B = R.f64(A), R.f64(B)
+        width, out = (cin, cout) if forward else (cout, cin)
+        data = (b["x"] if forward else b["dy"])[:, :width]
+        got = torch.full((b["T"], out), 7.0, dtype=torch.bfloat16, device="cuda")
+        if forward:
+            api.lora_fwd(data.cuda(), row, ad, *b["seg"], Y=got, V=V)
+            weight, first, second = R.decode(row), A, B
+        else:
+            dA, dB = api.lora_bwd(data.cuda(), torch.ones(b["T"], cin, dtype=torch.bfloat16, device="cuda"), V.clamp(-1, 1), col, ad,
+                                  *b["seg"], 5, dX=got)[1:]
+            assert dA.isfinite().all() and dB.isfinite().all()
+            weight, first, second = R.decode(col), B.transpose(0, 2, 1), A.transpose(0, 2, 1)
+        codes = R.decode_bf16(data[:n].contiguous(), "row", **({} if forward else dict(sr=True, seed=5)))
+        d = R.f64(data)
+        d[n:] = 0
+        want, tol = _projected(b, d, first, second, codes, weight, TERMS)
+        # the decode scale is an FP32 product: half of a subnormal's step, times the sum of the code products; and half
+        # of a BF16 subnormal's step in the output, and of an FP32 one's in each low-rank product
+        sa, sb = float(O.global_scales(O.amax(data[:n].contiguous()))[1]), float(row.global_scale)
+        tol = tol + 2.0 ** -150 * (np.abs(codes) / sa) @ (np.abs(weight) / sb).T + 2.0 ** -134 + rank * 2.0 ** -149
+        R.assert_within(R.f64(got)[:n], want, tol, f"forward {forward}")
+        assert (got[n:] == 7.0).all()
