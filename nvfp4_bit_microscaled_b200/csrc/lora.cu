@@ -599,9 +599,9 @@ lora_grad_kernel(GradSide da, GradSide db, int rank, const int* sorted, const in
     for (int u = tid; u < 64 * MT * 4; u += 128) {
       const int r = u / (MT * 4), j = u % (MT * 4) * 4;
       const float4 v = *reinterpret_cast<const float4*>(gen + (done % STAGES) * STAGE + Z_TILE + u * 16);
-      const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-      const float2 fa = __bfloat1622float2(a), fb = __bfloat1622float2(b);
-      const __nv_bfloat162 c = __floats2bfloat162_rn(v.x - fa.x, v.y - fa.y), d = __floats2bfloat162_rn(v.z - fb.x, v.w - fb.y);
+      __nv_bfloat162 a, b, c, d;
+      split_bf16x2(make_float2(v.x, v.y), &a, &c);
+      split_bf16x2(make_float2(v.z, v.w), &b, &d);
       *reinterpret_cast<uint2*>(hi + r * P_PITCH + j * 2) =
           make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
       *reinterpret_cast<uint2*>(lo + r * P_PITCH + j * 2) =

@@ -244,3 +244,26 @@ def test_low_rank_sums_where_the_decode_scale_is_small(name, lengths, ids, cin, 
         tol = tol + 2.0 ** -150 * (np.abs(codes) / sa) @ (np.abs(weight) / sb).T + 2.0 ** -134 + rank * 2.0 ** -149
         R.assert_within(R.f64(got)[:n], want, tol, f"forward {forward}")
         assert (got[n:] == 7.0).all()
+
+
+@pytest.mark.parametrize("bad", [float("inf"), -3.39e38])
+@pytest.mark.parametrize("others", [2, 300])
+def test_infinite_sums_have_infinite_gradients(others, bad):
+    # an adapter of a single row: its gradients are products of two numbers, and where U or V is infinite so are they,
+    # with their sign.  -3.39e38, BF16's lowest, makes sums that FP32 cannot hold either
+    b = G._make([others, 1], [0, 1], 128, 192, 16, 2)
+    n = b["n"]
+    A, B = b["A"].clone(), b["B"].clone()
+    A[1, 3, 7], B[1, 5, 9] = bad, bad
+    x, dy = b["X"].clone(), b["dY"].clone()
+    x[n - 1, 7], dy[n - 1, 5] = 32.0, -64.0
+    ad = api.LoraAdapters(A.cuda(), B.cuda(), b["ad"].scale)
+    V = torch.zeros(b["T"], 16, device="cuda")
+    api.lora_fwd(x, b["row"], ad, *b["seg"], V=V)
+    assert V[n - 1, 3].item() == np.sign(bad) * np.inf and V[n - 1, [i for i in range(16) if i != 3]].isfinite().all()
+    _, dA, dB = api.lora_bwd(dy, x, V, b["col"], ad, *b["seg"], 1)
+    for got, j, z, sign in ((dA[1], 9, x[n - 1], -np.sign(bad)), (dB[1].t(), 3, dy[n - 1], np.sign(bad))):
+        got, z = R.f64(got), R.f64(z)
+        assert (got[j][z != 0] == sign * np.sign(z[z != 0]) * np.inf).all()
+        assert np.isfinite(np.delete(got, j, 0)).all()
+    assert dA[0].isfinite().all() and dB[0].isfinite().all()
