@@ -265,8 +265,8 @@ nvfp4_status nvfp4_linear_bwd(const void* dY, int64_t T, int64_t Cin, int64_t Co
  *
  * nvfp4_gated_apply: serving.  BF16 rows by a weight that was quantized once:
  *   makes X's per-tensor amax and row copy in the workspace and multiplies.
- *   X         device BF16 [T, C], row pitch ldx (ldx % 8 == 0).  T may be 0
- *             (nothing is done).
+ *   X         device BF16 [T, C], row pitch ldx (ldx % 8 == 0), C below 2^24.
+ *             T may be 0 (nothing is done).
  *   Up to 128 rows W is read once at HBM speed by tiles that hold all rows.
  *
  * nvfp4_gated_fwd / nvfp4_gated_bwd: training, as nvfp4_linear_fwd / _bwd (T and

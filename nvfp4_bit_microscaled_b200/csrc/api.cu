@@ -515,10 +515,12 @@ nvfp4_status nvfp4_gated_gemm(const nvfp4_tensor* A, const nvfp4_tensor* W, nvfp
 }
 
 // Workspace of nvfp4_gated_apply: decode scale, maxima, then X's row copy.
+// C below 2^24: the quantizer of few rows counts their blocks in 32 bits.
+constexpr int64_t kApplyColumns = int64_t(1) << 24;
 static size_t apply_header() { return 256 + align256(nvfp4::kRowMaxima * 4); }
 size_t nvfp4_gated_apply_workspace_bytes(int64_t T, int64_t C) {
   const int64_t lim = int64_t(1) << 31;
-  if (T <= 0 || C <= 0 || T >= lim || C >= lim) return 0;
+  if (T <= 0 || C <= 0 || T >= lim || C >= kApplyColumns) return 0;
   return apply_header() + align256(nvfp4_data_bytes(T, C)) + align256(nvfp4_scale_bytes(T, C));
 }
 
@@ -526,7 +528,7 @@ nvfp4_status nvfp4_gated_apply(const void* X, int64_t T, int64_t ldx, const nvfp
                                int64_t ldh, void* workspace, size_t workspace_bytes, nvfp4_stream_t stream) {
   if (!W || !act_ok(act)) return NVFP4_ERR_INVALID_ARG;
   const int64_t C = W->cols, F = W->rows / 2, lim = int64_t(1) << 31;
-  if (T < 0 || T >= lim || C <= 0 || C >= lim || C % 64 || W->rows <= 0 || W->rows >= lim || W->rows % 256 || ldx < C ||
+  if (T < 0 || T >= lim || C <= 0 || C >= kApplyColumns || C % 64 || W->rows <= 0 || W->rows >= lim || W->rows % 256 || ldx < C ||
       ldh < F)
     return NVFP4_ERR_SHAPE;
   nvfp4_status st;
