@@ -270,8 +270,8 @@ nvfp4_status nvfp4_linear_bwd(const void* dY, int64_t T, int64_t Cin, int64_t Co
  *   Up to 128 rows W is read once at HBM speed by tiles that hold all rows.
  *
  * nvfp4_gated_fwd / nvfp4_gated_bwd: training, as nvfp4_linear_fwd / _bwd (T and
- *   C multiples of 64, F below 2^24; both use the same side stream, with its
- *   capture rules).  The workspace is that of a linear layer with Cout = 2F and
+ *   C multiples of 64, F below 2^24, T 2F below 2^36; both use the same side
+ *   stream, with its capture rules).  The workspace is that of a linear layer with Cout = 2F and
  *   holds the same six operands; the forward leaves X's column copy and W's in
  *   it.
  *   GU        BF16 [T, 2F] contiguous: written by the forward, read by the

@@ -555,14 +555,20 @@ nvfp4_status nvfp4_gated_apply(const void* X, int64_t T, int64_t ldx, const nvfp
 }
 
 // The operands of a gated projection are those of a linear layer with Cout = 2F.
+// F below 2^24: offsets in a 64-row tile stay in 32 bits.  Fewer than 2^36
+// gradients: their blocks are counted in 32 bits (more of them, with dH, do not
+// fit in 180 GB).
+static bool gated_sizes_ok(int64_t T, int64_t F) {
+  return F > 0 && F < (int64_t(1) << 24) && T < (int64_t(1) << 31) && T * 2 * F < (int64_t(1) << 36);
+}
 static nvfp4_status gated_check(int64_t T, int64_t C, int64_t F, nvfp4_activation act, void* ws, size_t ws_bytes) {
   if (!act_ok(act)) return NVFP4_ERR_INVALID_ARG;
-  if (F <= 0 || F >= (int64_t(1) << 24) || F % 128) return NVFP4_ERR_SHAPE;   // offsets in a 64-row tile stay in 32 bits
+  if (!gated_sizes_ok(T, F) || F % 128) return NVFP4_ERR_SHAPE;
   return linear_check(T, C, 2 * F, ws, ws_bytes);
 }
 
 size_t nvfp4_gated_workspace_bytes(int64_t T, int64_t C, int64_t F) {
-  return F > 0 && F < (int64_t(1) << 24) ? nvfp4_linear_workspace_bytes(T, C, 2 * F) : 0;
+  return gated_sizes_ok(T, F) ? nvfp4_linear_workspace_bytes(T, C, 2 * F) : 0;
 }
 
 nvfp4_status nvfp4_gated_fwd(const void* X, const void* W, int64_t T, int64_t C, int64_t F, nvfp4_activation act, void* H,

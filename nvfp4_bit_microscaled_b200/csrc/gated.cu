@@ -154,7 +154,7 @@ __device__ __forceinline__ uint32_t grad_slot(int token, int block, int chunk) {
   return static_cast<uint32_t>(token * (kTileChannels * 4) + ((4 * block + (chunk ^ ((block >> 1) & 3))) << 4));
 }
 
-template <int ACT, bool NARROW>
+template <int ACT>
 __global__ void __launch_bounds__(256, 2) gated_grad_quant_kernel(
     const uint16_t* __restrict__ dh, const uint16_t* __restrict__ gu, int64_t T, int64_t F, const float* amax_dev,
     uint32_t k0, uint32_t k1, uint8_t* __restrict__ row_data, uint8_t* __restrict__ row_sf, float* __restrict__ row_gs,
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(256, 2) gated_grad_quant_kernel(
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           auto e = [&](int i) { return c ? v[p][i].y : v[p][i].x; };
-          const u32x4 w = sr_words<NARROW>(gb + c, kDomainColSR, k0, k1);
+          const u32x4 w = sr_words<true>(gb + c, kDomainColSR, k0, k1);
           *reinterpret_cast<uint2*>(dst + 32 * c) = make_uint2(
               clear_negative_zero(sr_e2m1x4(e(0), e(1), e(2), e(3), w.x) | (sr_e2m1x4(e(4), e(5), e(6), e(7), w.y) << 16)),
               clear_negative_zero(sr_e2m1x4(e(8), e(9), e(10), e(11), w.z) | (sr_e2m1x4(e(12), e(13), e(14), e(15), w.w) << 16)));
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(256, 2) gated_grad_quant_kernel(
 #pragma unroll
         for (int i = 0; i < 8; ++i) y[i] = __fmul2_rn(y[i], r2);
         const int64_t t = q * 64 + token, blk = p * (F >> 4) + cb * 8 + b;
-        const u32x4 w = sr_words<NARROW>(static_cast<uint64_t>(t * row_s + blk), kDomainRowSR, k0, k1);
+        const u32x4 w = sr_words<true>(static_cast<uint64_t>(t * row_s + blk), kDomainRowSR, k0, k1);
         *reinterpret_cast<uint2*>(row_data + t * F + blk * 8) = make_uint2(
             clear_negative_zero(sr_e2m1x4(y[0].x, y[0].y, y[1].x, y[1].y, w.x) |
                                 (sr_e2m1x4(y[2].x, y[2].y, y[3].x, y[3].y, w.y) << 16)),
@@ -293,10 +293,8 @@ cudaError_t launch_gated_grad_quant(const void* dH, const void* GU, int64_t T, i
                         amax, k0, k1, static_cast<uint8_t*>(row_data), static_cast<uint8_t*>(row_scales), row_gs,
                         static_cast<uint8_t*>(col_data), static_cast<uint8_t*>(col_scales), col_gs);
   };
-  static SmemOptIn opts[4];
-  const bool narrow = T * 2 * F < (int64_t(1) << 36);   // every block counter fits in 32 bits
-  if (act) return narrow ? run(gated_grad_quant_kernel<1, true>, &opts[0]) : run(gated_grad_quant_kernel<1, false>, &opts[1]);
-  return narrow ? run(gated_grad_quant_kernel<0, true>, &opts[2]) : run(gated_grad_quant_kernel<0, false>, &opts[3]);
+  static SmemOptIn opts[2];
+  return act ? run(gated_grad_quant_kernel<1>, &opts[0]) : run(gated_grad_quant_kernel<0>, &opts[1]);
 }
 
 }  // namespace nvfp4
