@@ -207,7 +207,6 @@ lora_shrink_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
   __shared__ int sh[2];
   __shared__ uint64_t full[kShrinkMaxStages], empty[kShrinkMaxStages], acc_full;
   __shared__ uint32_t tmem_slot;
-  __shared__ volatile uint32_t abort_flag;
   const int slices = p.slices, slice = slices > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int item = blockIdx.x / slices;
   // the last CTAs make the plan's tiles and the checks, one each; these and every
@@ -242,7 +241,6 @@ lora_shrink_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
       mbar_init(&empty[i], 5);   // the MMAs' commit and four warps
     }
     mbar_init(&acc_full, 1);
-    abort_flag = 0;
     fence_barrier_init();
     prefetch_tmap(&tmX);
     prefetch_tmap(&tmA);
@@ -259,7 +257,7 @@ lora_shrink_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
     int stage = 0, last = 0;
     uint32_t phase = 0;
     for (int i = 0; i < nc; ++i) {
-      if (!mbar_wait(&empty[stage], phase ^ 1u, kErrWaitEmpty)) { abort_flag = 1; break; }
+      if (!mbar_wait(&empty[stage], phase ^ 1u, kErrWaitEmpty)) break;
       mbar_arrive_expect_tx(&full[stage], boxes * (X_TILE / 4) + (id >= 0 ? p.n_pad * 128 : 0));
       if (boxes == 4)
         tma_load_2d(smem + stage * stage_bytes, &tmX, &full[stage], (c0 + i) * 64, t0);
@@ -277,7 +275,7 @@ lora_shrink_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
     int stage = 0;
     uint32_t phase = 0;
     for (int i = 0; i < nc; ++i) {
-      if (!mbar_wait(&full[stage], phase, kErrWaitFull)) { abort_flag = 1; break; }
+      if (!mbar_wait(&full[stage], phase, kErrWaitFull)) break;
       tc_fence_after();
       if (id >= 0) {
         const uint32_t at = smem_u32(smem + stage * stage_bytes);
@@ -303,7 +301,7 @@ lora_shrink_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
     uint32_t phase = 0;
     const int row = tid - 64;
     for (int i = 0; i < nc; ++i) {
-      if (!mbar_wait(&full[stage], phase, kErrWaitFull)) { abort_flag = 1; break; }
+      if (!mbar_wait(&full[stage], phase, kErrWaitFull)) break;
       if (row < n) {
         const uint4* x = reinterpret_cast<const uint4*>(smem + stage * stage_bytes + row * 128);
         uint4 v[8];

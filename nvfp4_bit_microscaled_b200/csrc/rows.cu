@@ -73,7 +73,6 @@ project_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
   allow_next_kernel();   // the launch of the last tiles
   __shared__ uint64_t full[MAX_STAGES], empty[MAX_STAGES], sf_full[MAX_STAGES], acc_full;
   __shared__ uint32_t tmem_slot;
-  __shared__ volatile uint32_t abort_flag;
   __shared__ int ids[KEEP];   // ADAPTER: the adapters of a pass's rows of X
   // ring: W tiles, X tiles, then W's scale tiles (two for GATED) and X's
   constexpr uint32_t SFW_BYTES = (KIND == kGated ? 2 : 1) * SF_BYTES;
@@ -97,7 +96,6 @@ project_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
       mbar_init(&sf_full[s], 4);
     }
     mbar_init(&acc_full, 1);
-    abort_flag = 0;
     fence_barrier_init();
     prefetch_tmap(&tmW);
     prefetch_tmap(&tmX);
@@ -114,7 +112,7 @@ project_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
     int stage = 0, last = 0;
     uint32_t phase = 0;
     for (int i = 0; i < nk; ++i) {
-      if (!mbar_wait(&empty[stage], phase ^ 1u, kErrWaitEmpty)) { abort_flag = 1; break; }
+      if (!mbar_wait(&empty[stage], phase ^ 1u, kErrWaitEmpty)) break;
       const int kt = kt0 + i;
       const uint32_t sf = static_cast<uint32_t>(min(KB_PER_STAGE, katoms - kt * KB_PER_STAGE)) * 512u;
       mbar_arrive_expect_tx(&full[stage], A_BYTES + (KIND == kGated ? 2 : 1) * sf);
@@ -136,7 +134,7 @@ project_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
     int stage = 0, last = 0;
     uint32_t phase = 0;
     for (int i = 0; i < nk; ++i) {
-      if (!mbar_wait(&empty[stage], phase ^ 1u, kErrWaitEmpty)) { abort_flag = 1; break; }
+      if (!mbar_wait(&empty[stage], phase ^ 1u, kErrWaitEmpty)) break;
       const int kt = kt0 + i;
       const uint32_t sf = static_cast<uint32_t>(min(KB_PER_STAGE, katoms - kt * KB_PER_STAGE)) * 512u;
       mbar_arrive_expect_tx(&full[stage], p.b_bytes + sf);
@@ -155,7 +153,7 @@ project_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
     int stage = 0;
     uint32_t phase = 0;
     for (int i = 0; i < nk; ++i) {
-      if (!mbar_wait(&sf_full[stage], phase, kErrWaitFull)) { abort_flag = 1; break; }
+      if (!mbar_wait(&sf_full[stage], phase, kErrWaitFull)) break;
       tc_fence_after();
       const int nkb = min(KB_PER_STAGE, katoms - (kt0 + i) * KB_PER_STAGE);
       const uint64_t adesc = adesc0 + static_cast<uint64_t>(stage * (A_BYTES >> 4));
@@ -175,7 +173,7 @@ project_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
     int stage = 0;
     uint32_t phase = 0;
     for (int i = 0; i < nk; ++i) {
-      if (!mbar_wait(&full[stage], phase, kErrWaitFull)) { abort_flag = 1; break; }
+      if (!mbar_wait(&full[stage], phase, kErrWaitFull)) break;
       const int nkb = min(KB_PER_STAGE, katoms - (kt0 + i) * KB_PER_STAGE);
       const uint8_t* sw = sfw_ring + stage * SFW_BYTES + lane * 16;
       const uint8_t* sx = sfx_ring + stage * SF_BYTES + lane * 16;
