@@ -267,7 +267,7 @@ nvfp4_status nvfp4_linear_bwd(const void* dY, int64_t T, int64_t Cin, int64_t Co
  *   makes X's per-tensor amax and row copy in the workspace and multiplies.
  *   X         device BF16 [T, C], row pitch ldx (ldx % 8 == 0), C below 2^24.
  *             T may be 0 (nothing is done).
- *   Up to 128 rows W is read once at HBM speed by tiles that hold all rows.
+ *   Up to 128 rows W is read once, by tiles that hold all rows.
  *
  * nvfp4_gated_fwd / nvfp4_gated_bwd: training, as nvfp4_linear_fwd / _bwd (T and
  *   C multiples of 64, F below 2^24, T 2F below 2^36; both use the same side

@@ -9,12 +9,13 @@
 // computes the products in FP32, and nothing is rounded before the quantizer's
 // own rounding.  Storing the gradients as BF16 would cost 8 bytes for the pair
 // (written, read twice) on top of the same reads once.
-// The exponential, the hyperbolic tangent and the division are the accurate
-// ones: a gradient that is off in its last bit can change a random draw's
-// outcome, and with it a code by a whole step.
-// Measured (8192 tokens, F = 10240, SiLU; 503 MB of input): the maxima 139 us
-// (3.6 TB/s), the copies 300 us.  Both are bound by instructions: 38 for a pair
-// of gradients in the first kernel, issue slots 60-67% busy, DRAM 22-40%.  Input
+// The exponential and the hyperbolic tangent are CUDA's accurate ones, and the
+// sigmoid's reciprocal is the hardware's approximation after one Newton step
+// (within an ulp or two): a gradient that is off in its last bits can change a
+// random draw's outcome, and with it a code by a whole step.
+// Measured (8192 tokens, F = 10240, SiLU; 503 MB of input): the maxima 138 us
+// (3.6 TB/s), the copies 306 us.  Both are bound by instructions: 38 for a pair
+// of gradients in the first kernel, issue slots 57-67% busy, DRAM 19-38%.  Input
 // tiles that TMA brings ahead of time changed neither (137 and 330 us), nor did
 // twice the warps with half the channels each (141 and 350 us).
 #include "tile.cuh"

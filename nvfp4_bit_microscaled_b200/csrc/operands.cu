@@ -2,7 +2,7 @@
 // the per-tensor amax, the row copy, and for low-rank adapters the slabs.
 // Bound by memory: x is read twice (the second time from L2 where it fits) and
 // written at 9/32 of its size.  1777 x 5120: amax and copy 11 us; 8192 x 8192:
-// the copy and eight adapters' slabs 35 us after the amax (4.8 TB/s).
+// the copy and eight adapters' slabs 37 us after the amax (4.6 TB/s).
 #include "tile.cuh"
 
 namespace nvfp4 {

@@ -34,7 +34,8 @@
 // next tile's MMAs run.
 // Measured: GATED, 8192 x 5120 by 10240 + 10240, 352 us without G | U (4.9
 // PFLOP/s, the rate of the plain GEMM) and 380 with it; 1777 rows 88 us, tensor
-// pipe 58%.  ADAPTER, 8192 x 8192 x 8192, rank 64, eight adapters: 215 us.
+// pipe 58%.  ADAPTER, 8192 x 8192 x 8192, rank 64, eight adapters: 221 us (215
+// with V in one BF16 term).
 // Every mbarrier wait is bounded, as in gemm.cu.
 #define NVFP4_UNIT_ERROR_WORD   // compiled without relocatable device code, for setmaxnreg
 #include "tile.cuh"

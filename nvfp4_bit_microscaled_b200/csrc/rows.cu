@@ -27,10 +27,11 @@
 //                64 rows took twice as long as the loop); then they and warps
 //                2-5 write the output.
 // Measured, quantizer included: GATED, 5120 by 10240 + 10240 (59 MB of W), one
-// row 17.7 us, 48 rows 20.4 us; ADAPTER, 8192 x 8192, rank 16, 64 requests of
-// one row 19.0 us.  The kernel itself reads DRAM at 2.8 TB/s under ncu, from a
-// cold start to the last output; the rest is the quantizer in front (4 us), the
-// ring's filling and the join of the slices.
+// row 16.4 us, 48 rows 19.3 us; ADAPTER, 8192 x 8192, rank 16, 64 requests of
+// one row 19.3 us.  The kernel itself reads DRAM at 2.2 to 2.7 TB/s under ncu,
+// from a cold start to the last output; the rest is the quantizer in front (4
+// us).  The gated case has 160 tiles in one slice each: 160 CTAs for 296 places,
+// each walking 20 K steps through one chain of scales, MMA and commit.
 // W does not depend on the kernel before this one (the quantizer of X), so the
 // producer fills the ring with W before it waits for that kernel to finish
 // (programmatic dependent launch).

@@ -158,7 +158,9 @@ __device__ __forceinline__ void regs_claim() {
 // s = sigmoid(q(g)) with act(g) = g s: q(g) = g (SiLU) or, for the tanh form
 // of GELU, q(g) = 2 sqrt(2/pi) (g + 0.044715 g^3), as (1 + tanh z) / 2 =
 // sigmoid(2 z).  Beyond |g| = 30 both are 0 or 1 in FP32; the clamp keeps g^3
-// finite.  The fast exponential and division are within a few FP32 ulps.
+// finite.  The fast exponential's error grows with its argument, about |q| ulps,
+// and reaches the 90 or so where the sigmoid still differs from 0 or 1; the fast
+// division adds two.  128 ulps are a 512th of the rounding of H to BF16.
 constexpr float kGeluA = 1.5957691216057308f, kGeluB = 0.044715f;
 template <int ACT>
 __device__ __forceinline__ float gate_sigmoid(float g) {
